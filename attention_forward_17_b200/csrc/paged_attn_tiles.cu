@@ -316,7 +316,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 float vb = 0.f, c = cl;
                 if constexpr (FP8) {
                     const uint32_t f = 2 * ((unit_no + u) & 3);
-                    c = cl * bars->fac[f];
+                    // never 0, as it would be for a row of zeros over small keys: hidden scores are -inf, and
+                    // 0 times that is NaN.  |S| stays below 2^23, so at the least c every exponent is 0 to 2^-100.
+                    c = fmaxf(cl * bars->fac[f], 1.17549435e-38f);
                     vb = bars->fac[f + 1];
                 }
                 const bool masked = k0 + kBN > g.all[ti] || (k0 < g.none[ti] && k0 + kBN > p.sinks);
