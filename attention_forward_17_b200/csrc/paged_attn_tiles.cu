@@ -24,9 +24,12 @@
 //
 // e4m3 caches: four more warps widen each tile to f16 in shared memory.  A row is
 // multiplied by 2^(b - B + 6), B the largest b of the tile, which is exact while
-// b >= B - 21 (and loses the value below 2^-30 of the tile's largest); 2^(B - 6) then
-// belongs to the whole tile: K's goes into the factor of the scores, V's joins the exponent of
-// the weights as in the row kernel.  Q goes to f16 after a power-of-two scale per row.
+// b >= B - 21; 2^(B - 6) then belongs to the whole tile: K's goes into the factor of the scores, V's joins
+// the exponent of the weights as in the row kernel.  Q goes to f16 after a power-of-two scale per row.
+// Tiles whose scales lie further apart (K: 2^21; V: 2^8, since B also lifts the running maximum of rows
+// that do not see the largest row, and f16 weights have 22 bits of room below it) are widened
+// without their scales, and the softmax threads take each key's own (step_by_key).  Rows at the lowest scale,
+// zeros among them, may count as zeros and do not make a tile such.
 //
 // Measured on one B200 (device time): a 512-token chunk over 16,384 cached, 8 key heads of 4 query
 // heads, d = 128, bf16: 119 to 122 us with the join, 1,110 to 1,140 TFLOP/s, 0.67 to 0.69 of the measured cuBLAS burst.  A
@@ -50,6 +53,8 @@ namespace {
 
 constexpr int kRT = kTileRows, kBN = 128;
 constexpr int kProducer = 8, kIssuer = 9, kSched = 10, kWiden = 12;
+constexpr float kTauF16 = 15.f, kTopF16 = 8.f;     // f16 weights: the maximum's lag, and where a fresh one sits (base 2)
+constexpr int kSpanK = 21, kSpanV = 8;             // e4m3: scales of a tile that share a factor (base 2)
 
 template <int D, bool FP8>
 struct Cfg {
@@ -69,7 +74,7 @@ struct Cfg {
     static constexpr int kRawOff = kSlotOff + kSlots * kTileBytes;
     static constexpr int kExpOff = kRawOff + kRaws * kRawBytes;
     static constexpr int kBarOff = kExpOff + kRaws * kExpBytes;
-    static constexpr int kSmemBytes = 1024 + kBarOff + (FP8 ? 2048 : 640);
+    static constexpr int kSmemBytes = 1024 + kBarOff + (FP8 ? 3072 : 640);
     static_assert(kSmemBytes <= 232448 - 512, "shared memory per CTA");
     static constexpr uint32_t kColO = 256;
 };
@@ -90,8 +95,9 @@ struct Bars {
     TileSegment seg[2];
     uint32_t tmem_base;
     volatile uint32_t abort;
-    float fac[FP8 ? 8 : 1];              // e4m3: of unit u: K's tile factor (2 (u % 4)), V's exponent (+ 1)
-    int red[FP8 ? 16 : 1];               // largest exponents by warp, two units
+    float fac[FP8 ? 8 : 1];              // e4m3: of unit u: K's tile factor (2 (u % 4)), V's exponent (+ 1); 0: by key
+    uint32_t by_key[FP8 ? 4 : 1][2][FP8 ? 32 : 1];     // scale bytes of K and V of unit u % 4, if taken by key
+    int red[FP8 ? 16 : 1];               // largest exponents, and smallest << 8, by warp, two units
     float row_scale[FP8 ? 256 : 1];      // Q's power of two by row
 };
 
@@ -149,6 +155,80 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 // 2^x in f16, x <= 15: normal, subnormal or 0.
 __device__ __forceinline__ uint32_t f16_power(int x) {
     return x >= -14 ? static_cast<uint32_t>(x + 15) << 10 : x >= -24 ? 1u << (x + 24) : 0u;
+}
+
+// e4m3 tiles whose scales lie far apart: a softmax thread's whole step, with each key's own scales, in
+// short loops out of line (chunks of 4 sequences over 31,477 cached, d = 128, and 2,048 rows over 16,384, d = 64,
+// where no tile comes here: 576 and 378 us without it; 606 and 426 with it inlined; 580 and 393 called from the
+// step's own loop; 584 and 369 so.  1,515 us when every tile of the first comes here).  S becomes
+// t_j = s_j + b_j in place.  The row sees the keys below a of the tile that are not below b, or are below z.
+template <int D>
+__device__ __noinline__ void step_by_key(const uint32_t* ek, const uint32_t* ev, uint32_t ts, uint32_t to, int a, int b, int z,
+                                         float cl, bool rescale, uint32_t p_half, uint32_t p_full, float& m, float& l) {
+    const auto seen = [&](int j) { return bits_below(a - j) & (~bits_below(b - j) | bits_below(z - j)); };
+    float top = -INFINITY, sum = 0.f, alpha = 1.f;
+#pragma unroll 1
+    for (int j = 0; j < kBN; j += 16) {
+        uint32_t t[16];
+        tmem_ld32x16(ts + j, t);
+        tmem_wait_ld();
+        reg_fence16(t);
+        const uint32_t see = seen(j);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int e = ek[(j + k) >> 2] >> (8 * (k & 3)) & 0xff, f = ev[(j + k) >> 2] >> (8 * (k & 3)) & 0xff;
+            const float kf = __uint_as_float(static_cast<uint32_t>(max(e - 6, 0)) << 23);
+            float v = fmaf(__uint_as_float(t[k]), cl * kf, static_cast<float>(f - 133));
+            if (!(see & (1u << k))) v = -INFINITY;
+            t[k] = __float_as_uint(v);
+            top = fmaxf(top, v);
+        }
+        reg_fence16(t);
+        tmem_st16(ts + j, t);
+    }
+    tmem_wait_st();
+    if (top > m + kTauF16) {
+        alpha = ex2_approx(m - (top - kTopF16));
+        m = top - kTopF16;
+    }
+    if (rescale && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+        for (int j = 0; j < D; j += 16) {
+            uint32_t o[16];
+            tmem_ld32x16(to + j, o);
+            tmem_wait_ld();
+            reg_fence16(o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            reg_fence16(o);
+            tmem_st16(to + j, o);
+        }
+    }
+    const float off = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+    for (int j = 0; j < kBN; j += 16) {
+        uint32_t t[16], w[8];
+        tmem_ld32x16(ts + j, t);
+        tmem_wait_ld();
+        reg_fence16(t);
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+            const float w0 = ex2_approx(__uint_as_float(t[k]) - off), w1 = ex2_approx(__uint_as_float(t[k + 1]) - off);
+            const uint32_t f = ev[(j + k) >> 2] >> (8 * (k & 3));
+            // a hidden key's scale may be anything, but adds a finite 0
+            sum = fmaf(w0, __uint_as_float((260 - max(f & 0xff, 6u)) << 23), sum);
+            sum = fmaf(w1, __uint_as_float((260 - max(f >> 8 & 0xff, 6u)) << 23), sum);
+            w[k / 2] = pack_f16x2(w0, w1);
+        }
+        reg_fence8(w);
+        tmem_st8(ts + j / 2, w);                         // over scores that have been read
+        tmem_wait_st();
+        if (j == 80 || j == 112) {
+            tc_fence_before();
+            mbar_arrive(j == 80 ? p_half : p_full);
+        }
+    }
+    l = fmaf(l, alpha, sum);
 }
 
 template <int D, bool FP8>
@@ -223,7 +303,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         const uint32_t t_s = tmem + lane_w + 128u * ti;
         const uint32_t t_o = tmem + lane_w + C::kColO + static_cast<uint32_t>(D) * ti;
         const uint32_t qtile = base + ti * C::kTileBytes;
-        constexpr float kTau = FP8 ? 15.f : 32.f, kTop = FP8 ? 8.f : 0.f;
+        constexpr float kTau = FP8 ? kTauF16 : 32.f, kTop = FP8 ? kTopF16 : 0.f;
         uint32_t steps = 0, segs = 0;
         uint32_t done_o = 0;
         uint32_t unit_no = 0;                            // units of earlier segments (both tiles alike)
@@ -310,109 +390,122 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 
             float m = -INFINITY, l = 0.f, lh = 0.f;
             for (int u = 0; u < n; ++u, ++steps) {
-                const int k0 = key_tile(g, u) * kBN;
-                wait_bar(bar(bars->s_full[ti]), steps & 1, abort, p.status);
-                tc_fence_after();
-                float vb = 0.f, c = cl;
-                if constexpr (FP8) {
-                    const uint32_t f = 2 * ((unit_no + u) & 3);
-                    // never 0, as it would be for a row of zeros over small keys: hidden scores are -inf, and
-                    // 0 times that is NaN.  |S| stays below 2^23, so at the least c every exponent is 0 to 2^-100.
-                    c = fmaxf(cl * bars->fac[f], 1.17549435e-38f);
-                    vb = bars->fac[f + 1];
-                }
-                const bool masked = k0 + kBN > g.all[ti] || (k0 < g.none[ti] && k0 + kBN > p.sinks);
-                uint32_t s[128];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]));
-                tmem_wait_ld();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]));
-                if (masked) {
-                    // visible keys of this row: j < a + k0 and (j >= b + k0 or j < sinks)
-                    const int x = g.r0 + 128 * ti + r, pos = g.p0 + x / p.group;
-                    const int a = (x < g.r1 ? min(pos + 1, g.hi) : 0) - k0;
-                    const int b = (p.window == kNoWindow ? 0 : pos - p.window + 1) - k0, z = p.sinks - k0;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        // bit i: key 32 q + i is visible
-                        const uint32_t see = bits_below(a - 32 * q) & (~bits_below(b - 32 * q) | bits_below(z - 32 * q));
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (!(see & (1u << k))) s[32 * q + k] = __float_as_uint(-INFINITY);
+                // (the rare tile taken by key is left to the outer loop, which keeps its call out of this one)
+                for (; u < n; ++u, ++steps) {
+                    const int k0 = key_tile(g, u) * kBN;
+                    wait_bar(bar(bars->s_full[ti]), steps & 1, abort, p.status);
+                    tc_fence_after();
+                    float vb = 0.f, c = cl;
+                    if constexpr (FP8) {
+                        const uint32_t f = (unit_no + u) & 3;
+                        const float fk = bars->fac[2 * f];
+                        if (__builtin_expect(fk == 0.f, 0)) break;
+                        // never 0, as it would be for a row of zeros over small keys: hidden scores are -inf, and
+                        // 0 times that is NaN.  |S| stays below 2^23, so at the least c every exponent is 0 to 2^-100.
+                        c = fmaxf(cl * fk, 1.17549435e-38f);
+                        vb = bars->fac[2 * f + 1];
                     }
-                }
-                float xm[8];
+                    const bool masked = k0 + kBN > g.all[ti] || (k0 < g.none[ti] && k0 + kBN > p.sinks);
+                    uint32_t s[128];
 #pragma unroll
-                for (int ch = 0; ch < 8; ++ch) {
-                    xm[ch] = -INFINITY;
+                    for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]));
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 16; k += 2)
-                        xm[ch] = max3f(xm[ch], __uint_as_float(s[16 * ch + k]), __uint_as_float(s[16 * ch + k + 1]));
-                }
-                float mn = fmaxf(max3f(xm[0], xm[1], xm[2]), max3f(xm[3], xm[4], fmaxf(xm[5], max3f(xm[6], xm[7], xm[7])))) * c;
-                if constexpr (FP8) mn += vb;
-                const bool grow = mn > m + kTau;
-                float alpha = 1.f;
-                if (grow) {
-                    alpha = ex2_approx(m - (mn - kTop));
-                    m = mn - kTop;
-                    l *= alpha;
-                    lh *= alpha;
-                }
-                // this row's O holds the products of the segment's earlier tiles, all
-                // complete: S of this step was issued after them
-                if (__any_sync(0xffffffffu, grow && u > 0)) {
-#pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t o[32];
-                        tmem_ld32(t_o + 32 * q, o);
-                        tmem_wait_ld();
-                        reg_fence32(o);
+                    for (int q = 0; q < 4; ++q) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]));
+                    if (masked) {
+                        // visible keys of this row: j < a + k0 and (j >= b + k0 or j < sinks)
+                        const int x = g.r0 + 128 * ti + r, pos = g.p0 + x / p.group;
+                        const int a = (x < g.r1 ? min(pos + 1, g.hi) : 0) - k0;
+                        const int b = (p.window == kNoWindow ? 0 : pos - p.window + 1) - k0, z = p.sinks - k0;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        reg_fence32(o);
-                        tmem_st32(t_o + 32 * q, o);
-                    }
-                }
-                const float off = (FP8 ? vb : 0.f) - (m == -INFINITY ? 0.f : m);
-                const uint64_t c2 = f2(c, c), off2 = f2(off, off);
-                uint64_t la0 = 0, la1 = 0;
-                float hl0 = 0.f, hh0 = 0.f, hl1 = 0.f, hh1 = 0.f;
-                uint32_t pw[kW0];
+                        for (int q = 0; q < 4; ++q) {
+                            // bit i: key 32 q + i is visible
+                            const uint32_t see = bits_below(a - 32 * q) & (~bits_below(b - 32 * q) | bits_below(z - 32 * q));
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int k = 0; k < (h ? kW1 : kW0); ++k) {
-                        const int sk = 2 * ((h ? kW0 : 0) + k);
-                        const uint64_t xv = fma2(f2(__uint_as_float(s[sk]), __uint_as_float(s[sk + 1])), c2, off2);
-                        float e0, e1;
-                        f2_split(xv, e0, e1);
-                        const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
-                        const uint32_t w = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-                        if (k & 1) {
-                            la1 = add2(la1, f2(p0, p1));
-                            if constexpr (!FP8) add_bf16x2_halves(hl1, hh1, w);
-                        } else {
-                            la0 = add2(la0, f2(p0, p1));
-                            if constexpr (!FP8) add_bf16x2_halves(hl0, hh0, w);
+                            for (int k = 0; k < 32; ++k)
+                                if (!(see & (1u << k))) s[32 * q + k] = __float_as_uint(-INFINITY);
                         }
-                        pw[k] = w;
                     }
-                    if (h == 0)
-                        store_words<kW0>(t_s, pw);
+                    float xm[8];
+#pragma unroll
+                    for (int ch = 0; ch < 8; ++ch) {
+                        xm[ch] = -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2)
+                            xm[ch] = max3f(xm[ch], __uint_as_float(s[16 * ch + k]), __uint_as_float(s[16 * ch + k + 1]));
+                    }
+                    float mn = fmaxf(max3f(xm[0], xm[1], xm[2]), max3f(xm[3], xm[4], fmaxf(xm[5], max3f(xm[6], xm[7], xm[7])))) * c;
+                    if constexpr (FP8) mn += vb;
+                    const bool grow = mn > m + kTau;
+                    float alpha = 1.f;
+                    if (grow) {
+                        alpha = ex2_approx(m - (mn - kTop));
+                        m = mn - kTop;
+                        l *= alpha;
+                        lh *= alpha;
+                    }
+                    // this row's O holds the products of the segment's earlier tiles, all
+                    // complete: S of this step was issued after them
+                    if (__any_sync(0xffffffffu, grow && u > 0)) {
+#pragma unroll 1
+                        for (int q = 0; q < D / 32; ++q) {
+                            uint32_t o[32];
+                            tmem_ld32(t_o + 32 * q, o);
+                            tmem_wait_ld();
+                            reg_fence32(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            reg_fence32(o);
+                            tmem_st32(t_o + 32 * q, o);
+                        }
+                    }
+                    const float off = (FP8 ? vb : 0.f) - (m == -INFINITY ? 0.f : m);
+                    const uint64_t c2 = f2(c, c), off2 = f2(off, off);
+                    uint64_t la0 = 0, la1 = 0;
+                    float hl0 = 0.f, hh0 = 0.f, hl1 = 0.f, hh1 = 0.f;
+                    uint32_t pw[kW0];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int k = 0; k < (h ? kW1 : kW0); ++k) {
+                            const int sk = 2 * ((h ? kW0 : 0) + k);
+                            const uint64_t xv = fma2(f2(__uint_as_float(s[sk]), __uint_as_float(s[sk + 1])), c2, off2);
+                            float e0, e1;
+                            f2_split(xv, e0, e1);
+                            const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
+                            const uint32_t w = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+                            if (k & 1) {
+                                la1 = add2(la1, f2(p0, p1));
+                                if constexpr (!FP8) add_bf16x2_halves(hl1, hh1, w);
+                            } else {
+                                la0 = add2(la0, f2(p0, p1));
+                                if constexpr (!FP8) add_bf16x2_halves(hl0, hh0, w);
+                            }
+                            pw[k] = w;
+                        }
+                        if (h == 0)
+                            store_words<kW0>(t_s, pw);
+                        else
+                            store_words<kW1>(t_s + kW0, pw);
+                        tc_fence_before();
+                        mbar_arrive(bar(h == 0 ? bars->p_half[ti] : bars->p_full[ti]));
+                    }
+                    float v0, v1;
+                    f2_split(add2(la0, la1), v0, v1);
+                    if constexpr (FP8)
+                        l = fmaf(v0 + v1, __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(vb)) << 23), l);
                     else
-                        store_words<kW1>(t_s + kW0, pw);
-                    tc_fence_before();
-                    mbar_arrive(bar(h == 0 ? bars->p_half[ti] : bars->p_full[ti]));
+                        l += v0 + v1;
+                    lh += (hl0 + hh0) + (hl1 + hh1);
                 }
-                float v0, v1;
-                f2_split(add2(la0, la1), v0, v1);
-                if constexpr (FP8)
-                    l = fmaf(v0 + v1, __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(vb)) << 23), l);
-                else
-                    l += v0 + v1;
-                lh += (hl0 + hh0) + (hl1 + hh1);
+                if (!FP8 || u == n) break;
+                if constexpr (FP8) {
+                    const uint32_t f = (unit_no + u) & 3;
+                    const int k0 = key_tile(g, u) * kBN, x = g.r0 + 128 * ti + r, pos = g.p0 + x / p.group;
+                    step_by_key<D>(bars->by_key[f][0], bars->by_key[f][1], t_s, t_o, (x < g.r1 ? min(pos + 1, g.hi) : 0) - k0,
+                                   (p.window == kNoWindow ? 0 : pos - p.window + 1) - k0, p.sinks - k0, cl, u > 0,
+                                   bar(bars->p_half[ti]), bar(bars->p_full[ti]), m, l);
+                }
             }
             if constexpr (FP8) lh = l;
 
@@ -745,29 +838,41 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     uint32_t mul = mul_v;
                     if ((x & 1) == 0) {
                         live = alive(g, key_tile(g, x >> 1) * kBN + r);
-                        // the largest scales of the tile, of K and of V
+                        // the largest and smallest scales of the tile, of K and of V
                         const uint8_t* ex = smem + C::kExpOff + rs * C::kExpBytes + ((r >> pr_log2) << 7) + (r & (pr - 1));
                         const int ek = live ? min(static_cast<int>(ex[0]), 253) : 0;
                         const int ev = live ? min(static_cast<int>(ex[1024]), 253) : 0;
                         const int mk = __reduce_max_sync(0xffffffffu, ek), mv = __reduce_max_sync(0xffffffffu, ev);
+                        // (rows at the lowest scale, zeros among them, may count as zeros)
+                        const int nk = __reduce_min_sync(0xffffffffu, ek > 64 ? ek : 255);
+                        const int nv = __reduce_min_sync(0xffffffffu, ev > 64 ? ev : 255);
                         const int par = (i >> 1) & 1;
                         if (lane == 0) {
-                            bars->red[8 * par + w4] = mk;
-                            bars->red[8 * par + 4 + w4] = mv;
+                            bars->red[8 * par + w4] = mk | nk << 8;
+                            bars->red[8 * par + 4 + w4] = mv | nv << 8;
                         }
                         named_barrier_sync(3, 128);
-                        int tk = 64, tv = 64;
+                        int tk = 64, tv = 64, lk = 255, lv = 255;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            tk = max(tk, bars->red[8 * par + q]);
-                            tv = max(tv, bars->red[8 * par + 4 + q]);
+                            const int wk = bars->red[8 * par + q], wv = bars->red[8 * par + 4 + q];
+                            tk = max(tk, wk & 0xff);
+                            tv = max(tv, wv & 0xff);
+                            lk = min(lk, wk >> 8);
+                            lv = min(lv, wv >> 8);
                         }
-                        mul = f16_power(ek - tk + 6) * 0x10001u;
-                        mul_v = f16_power(ev - tv + 6) * 0x10001u;
+                        const uint32_t f = (i >> 1) & 3;
+                        // taken by key: codes times 2^6
+                        const bool by_key = tk > lk + kSpanK || tv > lv + kSpanV;
+                        mul = f16_power(by_key ? 6 : ek - tk + 6) * 0x10001u;
+                        mul_v = f16_power(by_key ? 6 : ev - tv + 6) * 0x10001u;
                         if (r == 0) {
-                            const uint32_t f = 2 * ((i >> 1) & 3);
-                            bars->fac[f] = __uint_as_float(static_cast<uint32_t>(tk - 6) << 23);
-                            bars->fac[f + 1] = static_cast<float>(tv - 6 - 127);
+                            bars->fac[2 * f] = by_key ? 0.f : __uint_as_float(static_cast<uint32_t>(tk - 6) << 23);
+                            bars->fac[2 * f + 1] = static_cast<float>(tv - 6 - 127);
+                        }
+                        if (by_key) {
+                            reinterpret_cast<uint8_t*>(bars->by_key[f][0])[r] = static_cast<uint8_t>(ek);
+                            reinterpret_cast<uint8_t*>(bars->by_key[f][1])[r] = static_cast<uint8_t>(ev);
                         }
                     }
                     if (i >= C::kSlots) wait_bar(bar(bars->kv_empty[s]), (i / C::kSlots - 1) & 1, abort, p.status);

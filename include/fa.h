@@ -437,7 +437,9 @@ int fa_kv_read(const fa_kv_cache* cache, const fa_kv_batch* batch, void* k, void
  * value for a row that does not see it.  (A value of V that is not finite may turn the output of a row that does
  * not see it into NaN when a neighbouring row of the same sequence does see it: zero times it is NaN.)
  * Products and sums: bf16 (16-bit float for an e4m3 cache) products with fp32 accumulation, fp32
- * softmax, weights rounded to 16 bits before the product with V.  Results do not depend on the
+ * softmax, weights rounded to 16 bits before the product with V.  With an e4m3 cache an element of Q below
+ * 2^-24 of its row's largest and a cached row at the lowest scale (e = 64: all of it below 2^-54) may count
+ * as zero; apart from that cached values enter as they are, whatever the sizes of other rows.  Results do not depend on the
  * order in which the GPU runs the parts.  Checks in the order of fa_kv_append (heads_q, window
  * and sinks with the sizes, scale after alignment, workspace_bytes too small: FA_ERR_SHAPE).
  */

@@ -49,3 +49,111 @@ def test_all_zeros_through_an_e4m3_cache(cuda_device, hint, d, n, kv):
     # LSE = ln 2 (m + log2 l): V's rows have the scale 2^-63, so |m| and log2 l are up to 80 while
     # the sum is small; l is exact, its logarithm good to 2^-22 of itself, and each rounds by 2^-24
     assert ((lse.double().cpu() - want).abs() <= 80 * (2.0 ** -22 + 2 * 2.0 ** -24)).all()
+
+
+
+# ------------------------------------------------------------------ rows that a query does not see
+def rescale(pr, x, s, p, by):
+    """Row p of sequence s times 2^by, in the cache's scales and in the 64-bit values."""
+    pg, row = int(pr.table[s, p // pr.page]), p % pr.page
+    pr.gpu[x + "e"][pg, :, row] += by
+    assert (pr.gpu[x + "e"][pg, :, row].int() - by == pr.cpu[x][1][pg, :, row].cuda().int()).all()
+    pr.dense[x][s][p] *= 2.0 ** by
+
+
+def reference(pr, news, kvs):
+    """The same problem with other lengths, and no GPU side."""
+    c = Problem.__new__(Problem)
+    c.__dict__.update(pr.__dict__)
+    c.news, c.kvs = news, kvs
+    c.dense = {x: [r[:t].clone() for r, t in zip(pr.dense[x], kvs)] for x in "kv"}
+    return c
+
+
+def compare(c, got, rows, by, window=0, sinks=0, what="", least=0.0):
+    """Packed rows `rows` of got against the 64-bit form of c, where rows of V lie up to 2^by apart.
+
+    Beside the bounds of attention(): LSE = ln 2 (m + log2 l), where m and -log2 l hold V's exponent (up to
+    |by| + 16) and cancel; the logarithm is good to 2^-22 of itself and each rounds by 2^-24.  A tile's scales may
+    differ by 2^8 before each key is taken by its own: weights are then f16 numbers that start at 2^0
+    instead of 2^8, of steps of 2^-24 at the least, so each is off by another 2^-25 of the sum."""
+    o, lse, bo, bl = c.attention(None, window, sinks)
+    bl = bl + (abs(by) + 16) * (2.0 ** -22 + 2 * 2.0 ** -24)
+    bo += least
+    for s, t in enumerate(c.kvs):
+        r0, r1 = int(c.cu[s]), int(c.cu[s + 1])
+        bo[r0:r1] += t * 2.0 ** -25 * max(c.dense["v"][s].abs().max().item(), 0.0)
+    go, gl = got[0].double().cpu()[rows], got[1].double().cpu()[rows]
+    assert torch.isfinite(go).all(), what
+    eo, el = (go - o[rows]).abs() - bo[rows], (gl - lse[rows]).abs() - bl[rows]
+    assert (eo <= 0).all(), f"{what}: O off by {eo.max().item():.3e} more than its bound, {(eo > 0).sum().item()} of {eo.numel()}"
+    assert (el <= 0).all(), f"{what}: LSE off by {el.max().item():.3e} more than its bound"
+
+
+@pytest.mark.gpu
+@HINT
+@pytest.mark.parametrize("x", ["k", "v"])
+@pytest.mark.parametrize("by", [6, 9, 12, 13, 20, 24, 32, 60])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_later_row_of_any_size_changes_nothing(cuda_device, hint, x, by, d):
+    # a row in the middle of a tile; the rows before it must come out as if it were not there
+    pr = Problem([200, 70], [200, 300], heads=2, group=2, d=d, fp8=True, page=32, seed=61)
+    rescale(pr, x, 0, 100, by)
+    rescale(pr, x, 1, 260, by)
+    got = fa.paged_attention(pr.q.cuda(), pr.cache, with_hint(pr, hint))
+    torch.cuda.synchronize()
+    c = reference(pr, [200, 70], [200, 300])
+    for s, p in ((0, 100), (1, 260)):
+        for y in "kv":
+            c.dense[y][s][p] = 0.0
+    before = torch.tensor(list(range(100)) + list(range(200, 230)))
+    compare(c, got, before, 0, what="rows before")
+    if x == "v":
+        compare(pr, got, torch.arange(270), by, what="all rows")
+
+
+@pytest.mark.gpu
+@HINT
+@pytest.mark.parametrize("by", [12, 24, 32, 60])
+def test_a_row_before_the_window_of_any_size_changes_nothing(cuda_device, hint, by):
+    pr = Problem([300], [400], heads=1, group=2, fp8=True, page=16, seed=62)
+    rescale(pr, "v", 0, 120, by)
+    got = fa.paged_attention(pr.q.cuda(), pr.cache, with_hint(pr, hint), window=64, sinks=5)
+    torch.cuda.synchronize()
+    c = reference(pr, [300], [400])
+    c.dense["v"][0][120] = 0.0
+    rows = torch.tensor([i for i in range(300) if not 120 <= 100 + i < 120 + 64])
+    compare(c, got, rows, 0, 64, 5, what="rows that do not see it")
+
+
+@pytest.mark.gpu
+@HINT
+@pytest.mark.parametrize("by", [-12, -21, -30, -50])
+def test_small_rows_beside_large_ones(cuda_device, hint, by):
+    # the first row sees the small one alone, the second that and a large one
+    pr = Problem([90], [90], heads=2, group=2, fp8=True, page=16, seed=63)
+    for x in "kv":
+        rescale(pr, x, 0, 0, by)
+    got = fa.paged_attention(pr.q.cuda(), pr.cache, with_hint(pr, hint))
+    torch.cuda.synchronize()
+    compare(pr, got, torch.arange(90), by, what="all rows")
+    v = pr.dense["v"][0][0].repeat_interleave(2, 0)
+    # one key: O is its row of V, which bf16 holds exactly
+    assert torch.equal(got[0][0].double().cpu(), v)
+
+
+@pytest.mark.gpu
+@HINT
+@pytest.mark.parametrize("x", ["k", "v"])
+def test_rows_at_the_lowest_scale(cuda_device, hint, x):
+    # they may count as zeros: 448 * 2^-63 < 2^-54 of O; of a score, nothing
+    pr = Problem([140, 1], [140, 70], heads=2, group=2, fp8=True, page=16, seed=65)
+    for s, p in ((0, 0), (0, 77), (0, 139), (1, 3), (1, 69)):
+        pg, row = int(pr.table[s, p // 16]), p % 16
+        for h in range(2):
+            by = 64 - int(pr.cpu[x][1][pg, h, row])
+            pr.gpu[x + "e"][pg, h, row] = 64
+            pr.dense[x][s][p, h] *= 2.0 ** by
+    got = fa.paged_attention(pr.q.cuda(), pr.cache, with_hint(pr, hint))
+    torch.cuda.synchronize()
+    compare(pr, got, torch.arange(141), 63, what="lowest scale", least=2.0 ** -54)
