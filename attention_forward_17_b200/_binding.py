@@ -445,8 +445,8 @@ class KVBatch:
     ``cu`` int32 [seqs + 1]: rows cu[s] .. cu[s+1]-1 of the packed tensors are the last of the
     ``kv_len[s]`` (int32 [seqs]) tokens of sequence s; ``table`` int32 [seqs, width]: the pages of each
     sequence in order.  All contiguous (table: rows may be strided) on one CUDA device, read
-    when the kernels run.  ``tokens`` is the number of rows of the packed tensors; rows from
-    cu[seqs] on are padding.  ``max_new`` is the largest number of new tokens of a sequence if known:
+    when the kernels run.  ``tokens`` is the number of rows of the packed tensors; rows before cu[0] and
+    from cu[seqs] on are padding.  ``max_new`` is the largest number of new tokens of a sequence if known:
     it chooses the kernels, which round in different places; any value gives right results.
     """
     __slots__ = ("cu", "kv_len", "table", "tokens", "device", "_struct", "_ref", "_sizes")
@@ -551,8 +551,8 @@ def kv_append(cache, batch, k, v, stream=None, status=None):
 def kv_read(cache, batch, out_k=None, out_v=None, stream=None, status=None):
     """Read the batch's rows back from the cache: (k, v), bf16 [tokens, heads, d].
 
-    ``out_k`` and ``out_v`` (equal strides) are allocated when not given; rows past cu[seqs] are
-    left as they are.  To read sequences whole pass a batch with n_s = kv_len[s].
+    ``out_k`` and ``out_v`` (equal strides) are allocated when not given; padding rows are left
+    as they are.  To read sequences whole pass a batch with n_s = kv_len[s].
     """
     _pair(cache, batch)
     if (out_k is None) != (out_v is None):
@@ -594,7 +594,7 @@ def paged_attention(q, cache, batch, scale: float | None = None, window: int = 0
     (bf16 of q's shape, own strides), ``lse`` (fp32 [tokens, heads_q]) and ``workspace`` (uint8,
     paged_attention_workspace() elements; one for each call that may run at the same time) are
     allocated when not given, on the stream the call runs on.  Rows that see no key get 0 and
-    -inf; rows past cu[seqs] are left as they are.  ``status`` (int32 CUDA tensor) receives FA_ERR_PAGE
+    -inf; padding rows are left as they are.  ``status`` (int32 CUDA tensor) receives FA_ERR_PAGE
     or FA_ERR_TIMEOUT.
     """
     _pair(cache, batch)

@@ -77,8 +77,8 @@ struct Cursor {
             end = 0x7fffffff;
             if (!padding) {
                 const Seq q = load_seq(b, s);
-                padding = t < q.row0;            // (only if cu decreases)
-                end = q.row0 + max(q.n, 1);
+                padding = t < q.row0;            // before the first sequence (or if cu decreases)
+                end = padding ? q.row0 : q.row0 + max(q.n, 1);
                 off = q.kv - q.n - q.row0;
                 table = b.table + s * b.table_stride;
                 at = -1;

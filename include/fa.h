@@ -359,8 +359,8 @@ int fa_kv_prepare(const fa_kv_cache* cache, void* out);
  * sequence s.  Row i of them sits at position p = kv_len[s] - n_s + i, which
  * the cache holds in row p % page_size of page table[s, p / page_size].
  *
- *   cu       device int32 [seqs + 1], not decreasing, cu[0] = 0 and cu[seqs] <= tokens; packed
- *            rows from cu[seqs] on are padding and are left as they are.
+ *   cu       device int32 [seqs + 1], not decreasing, 0 <= cu[0] and cu[seqs] <= tokens; packed
+ *            rows before cu[0] and from cu[seqs] on are padding and are left as they are.
  *   kv_len   device int32 [seqs].  A row whose position is negative (kv_len[s] < n_s) has no
  *            place in the cache: it is not written, reads as zeros and attends to nothing.
  *   table    device int32 [seqs, table_width], rows table_stride elements apart.

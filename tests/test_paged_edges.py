@@ -157,3 +157,34 @@ def test_rows_at_the_lowest_scale(cuda_device, hint, x):
     got = fa.paged_attention(pr.q.cuda(), pr.cache, with_hint(pr, hint))
     torch.cuda.synchronize()
     compare(pr, got, torch.arange(141), 63, what="lowest scale", least=2.0 ** -54)
+
+
+
+# ------------------------------------------------------------------ rows before the first sequence
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("heads", [1, 3, 8])
+@pytest.mark.parametrize("skip", [1, 3, 130])
+def test_packed_rows_before_the_first_sequence(cuda_device, fp8, heads, skip):
+    # some sequences of a larger batch: cu does not start at 0
+    pr = Problem([40, 0, 1, 90], [50, 7, 1, 200], heads=heads, d=64, page=16, fp8=fp8, seed=64, garbage=0)
+    T = pr.tokens + skip
+    cu = pr.batch.cu + skip
+    b = fa.KVBatch(cu, pr.batch.kv_len, pr.batch.table, T, 90)
+    new = {x: torch.cat([torch.full((skip, heads, 64), float("nan"), dtype=torch.bfloat16), pr.new[x]]).cuda() for x in "kv"}
+    other = Problem([40, 0, 1, 90], [50, 7, 1, 200], heads=heads, d=64, page=16, fp8=fp8, seed=64, garbage=0)
+    fa.kv_append(other.cache, other.batch, other.new["k"].cuda(), other.new["v"].cuda())
+    fa.kv_append(pr.cache, b, new["k"], new["v"])
+    got = [torch.full((T, heads, 64), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    fa.kv_read(pr.cache, b, *got)
+    q = torch.cat([torch.full((skip, 2 * heads, 64), float("nan"), dtype=torch.bfloat16), pr.q]).cuda()
+    out, lse = torch.full_like(q, 5.0), torch.full((T, 2 * heads), 5.0, device="cuda")
+    fa.paged_attention(q, pr.cache, b, out=out, lse=lse)
+    want = fa.kv_read(other.cache, other.batch)
+    o2, l2 = fa.paged_attention(pr.q.cuda(), other.cache, other.batch)
+    torch.cuda.synchronize()
+    for x, g, w in zip("kv", got, want):
+        assert torch.equal(pr.gpu[x].view(torch.uint8), other.gpu[x].view(torch.uint8)), x
+        assert (g[:skip] == 5.0).all() and torch.equal(g[skip:], w)
+    assert (out[:skip] == 5.0).all() and (lse[:skip] == 5.0).all()
+    assert torch.equal(out[skip:], o2) and torch.equal(lse[skip:], l2)
