@@ -19,14 +19,12 @@
 #pragma once
 
 #include "paged_common.cuh"
+#include "waits.cuh"
 
 namespace fa {
 namespace paged {
 
 constexpr int kNoWindow = 0x7fffffff;
-constexpr int kStatusTimeout = -7;                // FA_ERR_TIMEOUT
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
-constexpr uint64_t kWaitLimitAbortNs = 1000000ull;
 
 struct AttnParams {
     Batch b;
@@ -541,31 +539,15 @@ inline int launch_join_both(const AttnParams& rows, const AttnParams& tiles, cud
 }
 
 // ---------------------------------------------------------------- bounded waits
-__device__ __forceinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int* status) {
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return;
-        if ((i & 31u) == 0) {
-            const uint64_t limit = *abort ? kWaitLimitAbortNs : kWaitLimitNs;
-            if (global_timer_ns() - t0 > limit) {
-                if (!*abort) {
-                    *abort = 1u;
-                    if (status) atomicExch(status, kStatusTimeout);
-                }
-                return;
-            }
-        }
-    }
-}
 // For a single thread.
 __device__ __forceinline__ void wait_one(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int* status) {
-    if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, abort, status);
+    if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, abort, status, kWaitLimitNs, kWaitLimitAbortNs);
 }
 // For a whole warp.  Lanes may see the phase complete at different polls; they
 // meet again before the warp-collective instructions (ldmatrix, mma, tcgen05)
 // that follow a wait.
 __device__ __forceinline__ void wait_bar(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int* status) {
-    if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, abort, status);
+    if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, abort, status, kWaitLimitNs, kWaitLimitAbortNs);
     __syncwarp();
 }
 
