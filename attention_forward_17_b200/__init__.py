@@ -7,11 +7,11 @@ from ._binding import (FA_ERR_ALIGN, FA_ERR_ARCH, FA_ERR_ARG, FA_ERR_CUDA, FA_ER
                        KVBatch, KVCache, LIB_PATH, fa_fwd, fa_fwd_host, gemm, header_functions,
                        kv_append, kv_read, launches_per_call, lib, paged_attention,
                        paged_attention_workspace, pick_schedule,
-                       rescale_stats, row_softmax, schedules, selftest_wait_timeout, strerror, vector_add,
-                       version)
+                       rescale_stats, row_softmax, schedules, selftest_paged_attention_abandoned,
+                       selftest_wait_timeout, strerror, vector_add, version)
 
 __all__ = ["fa_fwd", "fa_fwd_host", "rescale_stats", "row_softmax", "gemm", "vector_add", "schedules",
-           "pick_schedule", "selftest_wait_timeout", "KVCache", "KVBatch", "kv_append", "kv_read",
+           "pick_schedule", "selftest_wait_timeout", "selftest_paged_attention_abandoned", "KVCache", "KVBatch", "kv_append", "kv_read",
            "paged_attention", "paged_attention_workspace",
            "FaError", "strerror", "version", "launches_per_call", "header_functions", "lib",
            "LIB_PATH", "FA_OK", "FA_ERR_NULL", "FA_ERR_SHAPE", "FA_ERR_HEADDIM", "FA_ERR_ALIGN",

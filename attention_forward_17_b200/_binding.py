@@ -105,6 +105,8 @@ def _load():
     lib.fa_paged_attn.argtypes = [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64,
                                   ctypes.c_float, _vp, _i64, _vp, _vp]
     lib.fa_paged_attn.restype = ctypes.c_int
+    lib.fa_selftest_paged_attn_abandoned.argtypes = lib.fa_paged_attn.argtypes
+    lib.fa_selftest_paged_attn_abandoned.restype = ctypes.c_int
     lib.fa_paged_attn_workspace.argtypes = [_vp, _vp, _i64]
     lib.fa_paged_attn_workspace.restype = _i64
     lib.fa_fwd_launches.argtypes = [_i64, _i64, _i64, _i64]
@@ -621,4 +623,21 @@ def paged_attention(q, cache, batch, scale: float | None = None, window: int = 0
                _status_ptr(status, device), _stream(stream, cache._index))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_attn")
+    return out, lse
+
+
+def selftest_paged_attention_abandoned(q, cache, batch, window: int = 0, sinks: int = 0):
+    """paged_attention as it goes on when a device-side wait has run out of time: LSE is NaN."""
+    _pair(cache, batch)
+    heads_q, device = q.shape[1], cache.device
+    qp, qts, qhs = _packed("q", q, batch.tokens, heads_q, cache.d, device)
+    out = _torch.empty_like(q)
+    lse = _torch.empty(batch.tokens, heads_q, dtype=_torch.float32, device=device)
+    workspace = _torch.empty(paged_attention_workspace(cache, batch, heads_q), dtype=_torch.uint8, device=device)
+    op, ots, ohs = _packed("out", out, batch.tokens, heads_q, cache.d, device)
+    rc = _call(cache._index, lib.fa_selftest_paged_attn_abandoned, qp, qts, qhs, op, ots, ohs, lse.data_ptr(), heads_q,
+               cache._ref, batch._ref, int(window), int(sinks), 1.0 / math.sqrt(cache.d), workspace.data_ptr(),
+               workspace.numel(), None, _raw_stream(cache._index))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_selftest_paged_attn_abandoned")
     return out, lse

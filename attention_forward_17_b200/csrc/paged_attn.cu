@@ -147,42 +147,11 @@ int64_t workspace_bytes_for(const fa_kv_cache* c, const fa_kv_batch* b, int64_t 
     return (a + 15) / 16 * 16 + t;           // the kernels may run at the same time
 }
 
-}  // namespace
-}  // namespace paged
-}  // namespace fa
-
-extern "C" int fa_kv_prepare(const fa_kv_cache* cache, void* out) {
-    using namespace fa::paged;
-    if (!cache) return FA_ERR_NULL;
-    int rc = check_cache_sizes(cache);
-    if (rc != FA_OK || (rc = check_cache_kind(cache)) != FA_OK) return rc;
-    if (!out || (rc = check_cache_pointers(cache)) != FA_OK) return FA_ERR_NULL;
-    if ((rc = check_cache_alignment(cache)) != FA_OK) return rc;
-    alignas(64) Prepared m;
-    if (encode_rows(m, cache) != FA_OK || encode_tiles(m, cache) != FA_OK) return FA_ERR_CUDA;
-    memcpy(out, &m, sizeof(m));
-    return FA_OK;
-}
-
-extern "C" int64_t fa_paged_attn_workspace(const fa_kv_cache* cache, const fa_kv_batch* batch, int64_t heads_q) {
-    using namespace fa::paged;
-    int rc = check_sizes(cache, batch);
-    if (rc < 0) return rc;
-    int rc2 = check_heads(cache, batch, heads_q);
-    if (rc2 != FA_OK) return rc2;
-    if (rc == 1) return 0;
-    int sms = 0;
-    if ((rc = device_ready(sms)) != FA_OK) return rc;
-    return workspace_bytes_for(cache, batch, heads_q, sms);
-}
-
-extern "C" int fa_paged_attn(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* o,
-                             int64_t o_token_stride, int64_t o_head_stride, float* lse, int64_t heads_q,
-                             const fa_kv_cache* cache, const fa_kv_batch* batch, int64_t window, int64_t sinks,
-                             float scale, void* workspace, int64_t workspace_bytes, int* dev_status,
-                             void* stream) {
-    using namespace fa::paged;
-    using fa::host::aligned;
+int attend(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* o, int64_t o_token_stride,
+           int64_t o_head_stride, float* lse, int64_t heads_q, const fa_kv_cache* cache, const fa_kv_batch* batch,
+           int64_t window, int64_t sinks, float scale, void* workspace, int64_t workspace_bytes, int* dev_status,
+           uint32_t abandoned, void* stream) {
+    using host::aligned;
     const int empty = check_sizes(cache, batch);
     if (empty < 0) return empty;
     int rc = check_heads(cache, batch, heads_q);
@@ -218,6 +187,7 @@ extern "C" int fa_paged_attn(const void* q, int64_t q_token_stride, int64_t q_he
     p.ctas = sms;
     p.whole = 0;
     p.after_rows = 0;
+    p.abandoned = abandoned;
     p.q_tma = p.group <= 128 && (p.group & (p.group - 1)) == 0;
     p.ws = static_cast<float*>(workspace);
     p.status = dev_status;
@@ -253,4 +223,52 @@ extern "C" int fa_paged_attn(const void* q, int64_t q_token_stride, int64_t q_he
             return rc;
     }
     return FA_OK;
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace fa
+
+extern "C" int fa_kv_prepare(const fa_kv_cache* cache, void* out) {
+    using namespace fa::paged;
+    if (!cache) return FA_ERR_NULL;
+    int rc = check_cache_sizes(cache);
+    if (rc != FA_OK || (rc = check_cache_kind(cache)) != FA_OK) return rc;
+    if (!out || (rc = check_cache_pointers(cache)) != FA_OK) return FA_ERR_NULL;
+    if ((rc = check_cache_alignment(cache)) != FA_OK) return rc;
+    alignas(64) Prepared m;
+    if (encode_rows(m, cache) != FA_OK || encode_tiles(m, cache) != FA_OK) return FA_ERR_CUDA;
+    memcpy(out, &m, sizeof(m));
+    return FA_OK;
+}
+
+extern "C" int64_t fa_paged_attn_workspace(const fa_kv_cache* cache, const fa_kv_batch* batch, int64_t heads_q) {
+    using namespace fa::paged;
+    int rc = check_sizes(cache, batch);
+    if (rc < 0) return rc;
+    int rc2 = check_heads(cache, batch, heads_q);
+    if (rc2 != FA_OK) return rc2;
+    if (rc == 1) return 0;
+    int sms = 0;
+    if ((rc = device_ready(sms)) != FA_OK) return rc;
+    return workspace_bytes_for(cache, batch, heads_q, sms);
+}
+
+extern "C" int fa_paged_attn(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* o,
+                             int64_t o_token_stride, int64_t o_head_stride, float* lse, int64_t heads_q,
+                             const fa_kv_cache* cache, const fa_kv_batch* batch, int64_t window, int64_t sinks,
+                             float scale, void* workspace, int64_t workspace_bytes, int* dev_status,
+                             void* stream) {
+    using namespace fa::paged;
+    return attend(q, q_token_stride, q_head_stride, o, o_token_stride, o_head_stride, lse, heads_q, cache, batch, window, sinks,
+                  scale, workspace, workspace_bytes, dev_status, 0, stream);
+}
+
+extern "C" int fa_selftest_paged_attn_abandoned(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* o,
+                                                int64_t o_token_stride, int64_t o_head_stride, float* lse, int64_t heads_q,
+                                                const fa_kv_cache* cache, const fa_kv_batch* batch, int64_t window,
+                                                int64_t sinks, float scale, void* workspace, int64_t workspace_bytes,
+                                                int* dev_status, void* stream) {
+    return fa::paged::attend(q, q_token_stride, q_head_stride, o, o_token_stride, o_head_stride, lse, heads_q, cache, batch,
+                             window, sinks, scale, workspace, workspace_bytes, dev_status, 1, stream);
 }

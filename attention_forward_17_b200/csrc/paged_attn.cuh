@@ -41,6 +41,7 @@ struct AttnParams {
     int after_rows;                     // tile kernel: may start while the row kernel of the call still runs
     int q_tma;                          // tile kernel: the group is a power of two up to 128
     int whole;                          // items are not cut: a part takes those that start in it
+    uint32_t abandoned;                 // self-test: 1, every CTA starts as if one of its waits had run out of time
     float* ws;
     int* status;
 };
@@ -549,6 +550,11 @@ __device__ __forceinline__ void wait_one(uint32_t bar, uint32_t parity, volatile
 __device__ __forceinline__ void wait_bar(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int* status) {
     if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, abort, status, kWaitLimitNs, kWaitLimitAbortNs);
     __syncwarp();
+}
+
+// What a row gets in place of its logarithm or sum when a wait of its CTA ran out of time.
+__device__ __forceinline__ float unless_aborted(float x, const volatile uint32_t* abort) {
+    return *abort ? __int_as_float(0x7fc00000) : x;
 }
 
 // ---------------------------------------------------------------- TMA over the pages

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(seg_full + 8 * i, 1);
             mbar_init(seg_empty + 8 * i, kConsumers + kProducers - 1);
         }
-        *abort = 0u;
+        *abort = p.abandoned;
         fence_barrier_init();
     }
     let_next_start();
@@ -721,12 +721,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 out.x = pack_bf16x2(a.x * inv, a.y * inv);
                 out.y = pack_bf16x2(a.z * inv, a.w * inv);
                 *reinterpret_cast<uint2*>(p.o + token * p.o_ts + head * p.o_hs + col) = out;
-                if (col == 0) p.lse[token * p.heads_q + head] = *abort ? __int_as_float(0x7fc00000) : lse_of(M, L);
+                if (col == 0) p.lse[token * p.heads_q + head] = unless_aborted(lse_of(M, L), abort);
             } else {
                 *reinterpret_cast<float4*>(slot + (col / 4 * RT + r) * 4) = a;
                 if (col == 0) {
                     slot[RT * D + r] = M;
-                    slot[RT * (D + 1) + r] = L;
+                    slot[RT * (D + 1) + r] = unless_aborted(L, abort);
                     slot[RT * (D + 2) + r] = LH;
                 }
             }

@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             mbar_init(bar(bars->seg_full[i]), 1);
             mbar_init(bar(bars->seg_empty[i]), FP8 ? 14 : 10);   // warps that read it
         }
-        bars->abort = 0u;
+        bars->abort = p.abandoned;
         fence_barrier_init();
     }
     if (warp == kSched) {
@@ -558,9 +558,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 }
                 __syncwarp();
                 if (mine) {
-                    float lse = lse_of(m, l);
-                    if (*abort) lse = __int_as_float(0x7fc00000);
-                    p.lse[token * p.heads_q + head] = lse;
+                    p.lse[token * p.heads_q + head] = unless_aborted(lse_of(m, l), abort);
                 }
             } else {
                 float* slot = slot_at<kRT, D>(p, blockIdx.x, g.slot);
@@ -580,7 +578,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 }
                 if (mine) {
                     slot[kRT * D + rr] = m;
-                    slot[kRT * (D + 1) + rr] = l;
+                    slot[kRT * (D + 1) + rr] = unless_aborted(l, abort);
                     slot[kRT * (D + 2) + rr] = lh;
                 }
             }

@@ -432,7 +432,8 @@ int fa_kv_read(const fa_kv_cache* cache, const fa_kv_batch* batch, void* k, void
  *   workspace  device, 16-byte aligned, fa_paged_attn_workspace() bytes, contents
  *            irrelevant; calls that may run at the same time need one each.
  *   dev_status  optional device int, never cleared: FA_ERR_PAGE when a visible key has no place
- *            (the rows that see it are then undefined), FA_ERR_TIMEOUT as in fa_fwd_status.
+ *            (the rows that see it are then undefined), FA_ERR_TIMEOUT as in fa_fwd_status: the
+ *            rows that the CTA involved works on, alone or with others, receive LSE = NaN.
  * Values at positions that no row of a call sees are never used, whatever they are, nor is a key's
  * value for a row that does not see it.  (A value of V that is not finite may turn the output of a row that does
  * not see it into NaN when a neighbouring row of the same sequence does see it: zero times it is NaN.)
@@ -448,6 +449,19 @@ int fa_paged_attn(const void* q, int64_t q_token_stride, int64_t q_head_stride, 
                   const fa_kv_cache* cache, const fa_kv_batch* batch, int64_t window, int64_t sinks,
                   float scale, void* workspace, int64_t workspace_bytes, int* dev_status,
                   void* stream);
+
+/*
+ * fa_selftest_paged_attn_abandoned - fa_paged_attn as it goes on when a pipeline wait of every CTA has run
+ * out of time (which fa_selftest_wait_timeout tests by itself): all rows that are not padding receive
+ * LSE = NaN, whether one CTA has them or several.  No wait runs out in it, and dev_status gets no
+ * FA_ERR_TIMEOUT.  Arguments and checks as fa_paged_attn.
+ */
+int fa_selftest_paged_attn_abandoned(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                     void* o, int64_t o_token_stride, int64_t o_head_stride,
+                                     float* lse, int64_t heads_q, const fa_kv_cache* cache,
+                                     const fa_kv_batch* batch, int64_t window, int64_t sinks,
+                                     float scale, void* workspace, int64_t workspace_bytes,
+                                     int* dev_status, void* stream);
 
 /* Bytes of workspace fa_paged_attn needs for these arguments on the current device, or a
  * negative status. */
