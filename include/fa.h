@@ -364,7 +364,7 @@ int fa_kv_prepare(const fa_kv_cache* cache, void* out);
  *   kv_len   device int32 [seqs].  A row whose position is negative (kv_len[s] < n_s) has no
  *            place in the cache: it is not written, reads as zeros and attends to nothing.
  *   table    device int32 [seqs, table_width], rows table_stride elements apart.
- *   seqs     0 .. 2^20;  tokens 0 .. 2^31 - 1024 (rows of the packed tensors).
+ *   seqs     0 .. 2^20;  tokens 0 .. 2^30 (rows of the packed tensors).
  *   table_width * page_size <= 2^30, and * heads <= 2^36.
  *   max_new  the largest n_s, if known (else `tokens`): chooses the kernels, which
  *            round in different places; any value gives right results.

@@ -1,8 +1,11 @@
 """Paged cache operators at the ends of their ranges."""
+import ctypes
+
 import pytest
 import torch
 
 import attention_forward_17_b200 as fa
+from attention_forward_17_b200 import _binding as bnd
 from paged_utils import Problem
 
 HINT = pytest.mark.parametrize("hint", [1, None], ids=["rows", "tiles"])      # which kernel takes long sequences
@@ -10,6 +13,21 @@ HINT = pytest.mark.parametrize("hint", [1, None], ids=["rows", "tiles"])      # 
 
 def with_hint(pr, hint):
     return fa.KVBatch(pr.batch.cu, pr.batch.kv_len, pr.batch.table, pr.tokens, hint)
+
+
+# ------------------------------------------------------------------ sizes (no GPU needed)
+def test_the_largest_number_of_tokens():
+    # a missing pointer is found after the sizes
+    def codes(tokens):
+        c = bnd._CacheStruct(None, None, None, None, 4, 1, 16, 64, 1024, 1024, 64, fa.FA_KV_BF16, None)
+        b = bnd._BatchStruct(64, 128, 256, 2, tokens, 4, 4, 2)
+        cr, br = ctypes.addressof(c), ctypes.addressof(b)
+        return (fa.lib.fa_kv_append(cr, br, 16, 16, 64, 64, None, None), fa.lib.fa_kv_read(cr, br, 16, 16, 64, 64, None, None),
+                fa.lib.fa_paged_attn(16, 64, 64, 16, 64, 64, 16, 1, cr, br, 0, 0, 1.0, 16, 0, None, None))
+    assert codes(2 ** 30) == (fa.FA_ERR_NULL,) * 3
+    assert codes(2 ** 30 + 1) == (fa.FA_ERR_SHAPE,) * 3
+    text = open(bnd.HEADER).read()
+    assert "tokens 0 .. 2^30 (" in text
 
 
 # ------------------------------------------------------------------ queries and keys of zeros
