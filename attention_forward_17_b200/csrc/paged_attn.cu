@@ -80,30 +80,10 @@ int encode_q(CUtensorMap* map, const AttnParams& p, int64_t d) {
 
 namespace {
 
-struct DeviceState {
-    std::once_flag once;
-    int status = FA_OK;
-    int sms = 0;
-};
 DeviceState g_dev[kMaxDevices];
 
 int device_ready(int& sms) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
-    DeviceState& st = g_dev[dev];
-    std::call_once(st.once, [&] {
-        int major = 0, minor = 0;
-        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&st.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            st.status = FA_ERR_CUDA;
-        else if (major != 10 || minor != 0)
-            st.status = FA_ERR_ARCH;
-        else
-            st.status = rows_setup() == FA_OK ? tiles_setup() : FA_ERR_CUDA;
-    });
-    sms = st.sms;
-    return st.status;
+    return device_ready(g_dev, sms, [] { return rows_setup() == FA_OK ? tiles_setup() : FA_ERR_CUDA; });
 }
 
 // Contexts of at most this many keys are not cut by the row kernel: one unit of 32 for each of its 8

@@ -45,6 +45,33 @@ __device__ __forceinline__ void report_page(int* status) {
 // ---------------------------------------------------------------- host side
 constexpr int kMaxDevices = 64;
 
+struct DeviceState {
+    std::once_flag once;
+    int status = FA_OK;
+    int sms = 0;
+};
+// The current device's number of SMs, and what became of its check (compute capability 10.0: the code is
+// sm_100a) and of `setup`, both made once.
+template <class Setup>
+inline int device_ready(DeviceState (&states)[kMaxDevices], int& sms, Setup setup) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
+    DeviceState& st = states[dev];
+    std::call_once(st.once, [&] {
+        int major = 0, minor = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&st.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            st.status = FA_ERR_CUDA;
+        else if (major != 10 || minor != 0)
+            st.status = FA_ERR_ARCH;
+        else
+            st.status = setup();
+    });
+    sms = st.sms;
+    return st.status;
+}
+
 inline int check_cache_sizes(const fa_kv_cache* c) {
     if (c->pages < 1 || c->pages > 0x7fffffffLL || c->heads < 1 || c->heads > 65535) return FA_ERR_SHAPE;
     if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128 &&

@@ -247,28 +247,7 @@ __global__ void __launch_bounds__(kThreads, APPEND ? 6 : 5) kv_kernel(const __gr
     }
 }
 
-struct DeviceState {
-    std::once_flag once;
-    int status = FA_OK;
-    int sms = 0;
-};
 DeviceState g_dev[kMaxDevices];
-
-int device_ready(int& sms) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
-    DeviceState& st = g_dev[dev];
-    std::call_once(st.once, [&] {
-        int major = 0;
-        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&st.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            st.status = FA_ERR_CUDA;
-        else if (major != 10)
-            st.status = FA_ERR_ARCH;
-    });
-    sms = st.sms;
-    return st.status;
-}
 
 template <int D, bool FP8, bool APPEND>
 void launch(const KvParams& p, int tokens, unsigned grid, cudaStream_t s) {
@@ -293,7 +272,7 @@ int run(const fa_kv_cache* c, const fa_kv_batch* b, const void* k, const void* v
         !packed_ok(v, token_stride, head_stride, b->tokens, c->heads) || !host::aligned(dev_status, 4))
         return FA_ERR_ALIGN;
     int sms = 0;
-    if ((rc = device_ready(sms)) != FA_OK) return rc;
+    if ((rc = device_ready(g_dev, sms, [] { return int(FA_OK); })) != FA_OK) return rc;
     const bool fp8 = c->type == FA_KV_E4M3;
     const int64_t item = fp8 ? 1 : 2;
     KvParams p;
