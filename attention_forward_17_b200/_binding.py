@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 import re
 
@@ -384,8 +385,13 @@ def _need_torch():
     return _torch
 
 
+def _fixed(name):
+    """A read-only attribute: handles hold addresses, so a tensor set later would not be the one in use."""
+    return property(operator.attrgetter("_" + name))
+
+
 class KVCache:
-    """The paged keys and values of one layer (a handle; the tensors stay the caller's).
+    """The paged keys and values of one layer (a handle; the tensors stay the caller's, and are the same for its life).
 
     ``k`` and ``v`` are CUDA tensors [pages, heads, page_size, d] of equal shape and strides, bf16 or
     float8_e4m3fn, unit stride along d, any order of the other dimensions (pass
@@ -393,7 +399,8 @@ class KVCache:
     ``k_exp`` and ``v_exp``, contiguous uint8 [pages, heads, page_size]: a row's scale is 2^(e - 127).
     page_size is 16, 32, 64, 128 or 256, d 64 or 128.
     """
-    __slots__ = ("k", "v", "k_exp", "v_exp", "device", "heads", "d", "_struct", "_ref", "_index", "_prepared")
+    __slots__ = ("_k", "_v", "_k_exp", "_v_exp", "_device", "_heads", "_d", "_struct", "_ref", "_index", "_prepared")
+    k, v, k_exp, v_exp, device, heads, d = map(_fixed, ("k", "v", "k_exp", "v_exp", "device", "heads", "d"))
 
     def __init__(self, k, v, k_exp=None, v_exp=None):
         torch = _need_torch()
@@ -416,8 +423,8 @@ class KVCache:
             elif (not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.shape != k.shape[:3]
                   or not t.is_contiguous() or t.device != k.device):
                 raise ValueError(f"{name} must be a contiguous uint8 [pages, heads, page_size] tensor on the cache's device")
-        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
-        self.device, self.heads, self.d, self._index = k.device, k.shape[1], k.shape[3], k.device.index
+        self._k, self._v, self._k_exp, self._v_exp = k, v, k_exp, v_exp
+        self._device, self._heads, self._d, self._index = k.device, k.shape[1], k.shape[3], k.device.index
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if fp8 else None,
                                     v_exp.data_ptr() if fp8 else None, *k.shape, *k.stride()[:3],
                                     FA_KV_E4M3 if fp8 else FA_KV_BF16, None)
@@ -442,7 +449,7 @@ class KVCache:
 
 
 class KVBatch:
-    """The sequences of one step (a handle, used for every layer of the step).
+    """The sequences of one step (a handle, used for every layer of the step; its tensors may be written, not replaced).
 
     ``cu`` int32 [seqs + 1]: rows cu[s] .. cu[s+1]-1 of the packed tensors are the last of the
     ``kv_len[s]`` (int32 [seqs]) tokens of sequence s; ``table`` int32 [seqs, width]: the pages of each
@@ -451,7 +458,8 @@ class KVBatch:
     from cu[seqs] on are padding.  ``max_new`` is the largest number of new tokens of a sequence if known:
     it chooses the kernels, which round in different places; any value gives right results.
     """
-    __slots__ = ("cu", "kv_len", "table", "tokens", "device", "_struct", "_ref", "_sizes")
+    __slots__ = ("_cu", "_kv_len", "_table", "_tokens", "_device", "_struct", "_ref", "_sizes")
+    cu, kv_len, table, tokens, device = map(_fixed, ("cu", "kv_len", "table", "tokens", "device"))
 
     def __init__(self, cu, kv_len, table, tokens: int, max_new: int | None = None):
         torch = _need_torch()
@@ -469,11 +477,11 @@ class KVBatch:
             raise ValueError("cu and kv_len must be contiguous, and the rows of table")
         if tokens < 0 or (max_new is not None and max_new < 0):
             raise ValueError("tokens and max_new must not be negative")
-        self.cu, self.kv_len, self.table, self.tokens, self.device = cu, kv_len, table, int(tokens), cu.device
+        self._cu, self._kv_len, self._table, self._tokens, self._device = cu, kv_len, table, int(tokens), cu.device
         width = table.shape[1]
-        self._struct = _BatchStruct(cu.data_ptr(), kv_len.data_ptr(), table.data_ptr(), seqs, self.tokens, width,
+        self._struct = _BatchStruct(cu.data_ptr(), kv_len.data_ptr(), table.data_ptr(), seqs, self._tokens, width,
                                     table.stride(0) if seqs > 1 else width,
-                                    self.tokens if max_new is None else int(max_new))
+                                    self._tokens if max_new is None else int(max_new))
         self._ref = ctypes.addressof(self._struct)
         self._sizes = {}            # workspace bytes by (heads_q, heads, d), sizes only
 
@@ -493,7 +501,7 @@ def _packed(name, t, tokens, heads, d, device):
 def _pair(cache, batch):
     if not isinstance(cache, KVCache) or not isinstance(batch, KVBatch):
         raise TypeError("cache must be a KVCache and batch a KVBatch")
-    if batch.device != cache.device:
+    if batch._device != cache._device:
         raise ValueError("cache and batch must be on the same device")
 
 
@@ -540,12 +548,12 @@ def kv_append(cache, batch, k, v, stream=None, status=None):
     page lies outside the cache (that row is not written).
     """
     _pair(cache, batch)
-    kp, ts, hs = _packed("k", k, batch.tokens, cache.heads, cache.d, cache.device)
-    vp, ts2, hs2 = _packed("v", v, batch.tokens, cache.heads, cache.d, cache.device)
+    kp, ts, hs = _packed("k", k, batch._tokens, cache._heads, cache._d, cache._device)
+    vp, ts2, hs2 = _packed("v", v, batch._tokens, cache._heads, cache._d, cache._device)
     if (ts, hs) != (ts2, hs2):
         raise ValueError("k and v must have the same strides")
     rc = _call(cache._index, lib.fa_kv_append, cache._ref, batch._ref, kp, vp, ts, hs,
-               _status_ptr(status, cache.device), _stream(stream, cache._index))
+               _status_ptr(status, cache._device), _stream(stream, cache._index))
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_append")
 
@@ -560,14 +568,14 @@ def kv_read(cache, batch, out_k=None, out_v=None, stream=None, status=None):
     if (out_k is None) != (out_v is None):
         raise ValueError("give both out_k and out_v or neither")
     if out_k is None:
-        out_k = _on(stream, _torch.empty, batch.tokens, cache.heads, cache.d, dtype=_torch.bfloat16, device=cache.device)
+        out_k = _on(stream, _torch.empty, batch._tokens, cache._heads, cache._d, dtype=_torch.bfloat16, device=cache._device)
         out_v = _on(stream, _torch.empty_like, out_k)
-    kp, ts, hs = _packed("out_k", out_k, batch.tokens, cache.heads, cache.d, cache.device)
-    vp, ts2, hs2 = _packed("out_v", out_v, batch.tokens, cache.heads, cache.d, cache.device)
+    kp, ts, hs = _packed("out_k", out_k, batch._tokens, cache._heads, cache._d, cache._device)
+    vp, ts2, hs2 = _packed("out_v", out_v, batch._tokens, cache._heads, cache._d, cache._device)
     if (ts, hs) != (ts2, hs2):
         raise ValueError("out_k and out_v must have the same strides")
     rc = _call(cache._index, lib.fa_kv_read, cache._ref, batch._ref, kp, vp, ts, hs,
-               _status_ptr(status, cache.device), _stream(stream, cache._index))
+               _status_ptr(status, cache._device), _stream(stream, cache._index))
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_read")
     return out_k, out_v
@@ -576,7 +584,7 @@ def kv_read(cache, batch, out_k=None, out_v=None, stream=None, status=None):
 def paged_attention_workspace(cache, batch, heads_q: int) -> int:
     """Bytes of workspace paged_attention needs for this cache and batch."""
     _pair(cache, batch)
-    key = (heads_q, cache.heads, cache.d)
+    key = (heads_q, cache._heads, cache._d)
     n = batch._sizes.get(key)
     if n is None:
         n = _call(cache._index, lib.fa_paged_attn_workspace, cache._ref, batch._ref, heads_q)
@@ -602,19 +610,19 @@ def paged_attention(q, cache, batch, scale: float | None = None, window: int = 0
     _pair(cache, batch)
     if not isinstance(q, _torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [tokens, heads_q, d] tensor")
-    heads_q, device = q.shape[1], cache.device
-    qp, qts, qhs = _packed("q", q, batch.tokens, heads_q, cache.d, device)
+    heads_q, device = q.shape[1], cache._device
+    qp, qts, qhs = _packed("q", q, batch._tokens, heads_q, cache._d, device)
     if scale is None:
-        scale = 1.0 / math.sqrt(cache.d)
+        scale = 1.0 / math.sqrt(cache._d)
     bytes_ = paged_attention_workspace(cache, batch, heads_q)
     if out is None:
         out = _on(stream, _torch.empty_like, q)
     if lse is None:
-        lse = _on(stream, _torch.empty, batch.tokens, heads_q, dtype=_torch.float32, device=device)
+        lse = _on(stream, _torch.empty, batch._tokens, heads_q, dtype=_torch.float32, device=device)
     if workspace is None:
         workspace = _on(stream, _torch.empty, bytes_, dtype=_torch.uint8, device=device)
-    op, ots, ohs = _packed("out", out, batch.tokens, heads_q, cache.d, device)
-    if lse.dtype != _torch.float32 or lse.shape != (batch.tokens, heads_q) or not lse.is_contiguous() or lse.device != device:
+    op, ots, ohs = _packed("out", out, batch._tokens, heads_q, cache._d, device)
+    if lse.dtype != _torch.float32 or lse.shape != (batch._tokens, heads_q) or not lse.is_contiguous() or lse.device != device:
         raise ValueError("lse must be a contiguous fp32 [tokens, heads_q] tensor on the cache's device")
     if workspace.dtype != _torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
         raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
@@ -629,14 +637,14 @@ def paged_attention(q, cache, batch, scale: float | None = None, window: int = 0
 def selftest_paged_attention_abandoned(q, cache, batch, window: int = 0, sinks: int = 0):
     """paged_attention as it goes on when a device-side wait has run out of time: LSE is NaN."""
     _pair(cache, batch)
-    heads_q, device = q.shape[1], cache.device
-    qp, qts, qhs = _packed("q", q, batch.tokens, heads_q, cache.d, device)
+    heads_q, device = q.shape[1], cache._device
+    qp, qts, qhs = _packed("q", q, batch._tokens, heads_q, cache._d, device)
     out = _torch.empty_like(q)
-    lse = _torch.empty(batch.tokens, heads_q, dtype=_torch.float32, device=device)
+    lse = _torch.empty(batch._tokens, heads_q, dtype=_torch.float32, device=device)
     workspace = _torch.empty(paged_attention_workspace(cache, batch, heads_q), dtype=_torch.uint8, device=device)
-    op, ots, ohs = _packed("out", out, batch.tokens, heads_q, cache.d, device)
+    op, ots, ohs = _packed("out", out, batch._tokens, heads_q, cache._d, device)
     rc = _call(cache._index, lib.fa_selftest_paged_attn_abandoned, qp, qts, qhs, op, ots, ohs, lse.data_ptr(), heads_q,
-               cache._ref, batch._ref, int(window), int(sinks), 1.0 / math.sqrt(cache.d), workspace.data_ptr(),
+               cache._ref, batch._ref, int(window), int(sinks), 1.0 / math.sqrt(cache._d), workspace.data_ptr(),
                workspace.numel(), None, _raw_stream(cache._index))
     if rc != FA_OK:
         raise FaError(rc, "fa_selftest_paged_attn_abandoned")

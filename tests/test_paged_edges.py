@@ -206,3 +206,21 @@ def test_packed_rows_before_the_first_sequence(cuda_device, fp8, heads, skip):
         assert (g[:skip] == 5.0).all() and torch.equal(g[skip:], w)
     assert (out[:skip] == 5.0).all() and (lse[:skip] == 5.0).all()
     assert torch.equal(out[skip:], o2) and torch.equal(lse[skip:], l2)
+
+
+# ------------------------------------------------------------------ handles
+@pytest.mark.gpu
+def test_handles_do_not_take_other_tensors(cuda_device):
+    # the kernels would go on reading the old ones
+    pr = Problem([1, 3], [40, 70], fp8=True, seed=66)
+    for handle, names in ((pr.cache, ("k", "v", "k_exp", "v_exp", "heads", "d", "device")),
+                          (pr.batch, ("cu", "kv_len", "table", "tokens", "device"))):
+        for name in names:
+            with pytest.raises(AttributeError, match=name):
+                setattr(handle, name, getattr(handle, name))
+        with pytest.raises(AttributeError):
+            handle.other = 1
+    pr.batch.kv_len.copy_(torch.tensor([30, 60]))       # written in place: read by the next call
+    pr.dense = {x: [r[:t] for r, t in zip(pr.dense[x], (30, 60))] for x in "kv"}
+    pr.kvs = [30, 60]
+    pr.check(pr.run(), what="other lengths")
