@@ -178,6 +178,26 @@ def test_rows_at_the_lowest_scale(cuda_device, hint, x):
 
 
 
+@pytest.mark.gpu
+@HINT
+@pytest.mark.parametrize("news,kvs", [([1], [70]), ([1], [20000]), ([140], [140]), ([70, 1, 1], [700, 300, 20])])
+def test_large_values_beside_zeros(cuda_device, hint, news, kvs):
+    # the documented ends of V's range: magnitudes just below 2^48, and rows of zeros that keep their weight
+    pr = Problem(news, kvs, heads=1, group=2, fp8=True, page=64, seed=67)
+    for s, t in enumerate(kvs):
+        for p0 in range(0, t, 64):
+            pg, n = int(pr.table[s, p0 // 64]), min(64, t - p0)
+            pr.gpu["ve"][pg, :, :n] += 45
+            pr.gpu["v"].view(torch.uint8)[pg, :, 1:n:2] = 0
+            pr.gpu["ve"][pg, :, 1:n:2] = 64
+        pr.dense["v"][s] *= 2.0 ** 45
+        pr.dense["v"][s][1::2] = 0.0
+        assert pr.dense["v"][s].abs().max() < 2.0 ** 48
+    got = fa.paged_attention(pr.q.cuda(), pr.cache, with_hint(pr, hint))
+    torch.cuda.synchronize()
+    compare(pr, got, torch.arange(sum(news)), 108, what="large V")
+
+
 # ------------------------------------------------------------------ rows before the first sequence
 @pytest.mark.gpu
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
