@@ -542,10 +542,11 @@ def _on(stream, f, *args, **kw):
 def kv_append(cache, batch, k, v, stream=None, status=None):
     """Write the new tokens' keys and values, bf16 [tokens, heads, d], into the cache's pages.
 
-    Token and head strides are free (multiples of 8 elements, the same for k and v).  An e4m3 cache
+    Token and head strides are free (positive multiples of 8 elements, the same for k and v).  An e4m3 cache
     stores each row divided by the smallest power of two that brings it within +-448.  No two
     rows may have the same place.  ``status`` (int32 CUDA tensor) receives FA_ERR_PAGE if a row's
-    page lies outside the cache (that row is not written).
+    page lies outside the cache (that row is not written).  As in the other calls, tensors used on a ``stream``
+    that is not their own have to live until it is done with them (``Tensor.record_stream``).
     """
     _pair(cache, batch)
     kp, ts, hs = _packed("k", k, batch._tokens, cache._heads, cache._d, cache._device)
@@ -601,7 +602,7 @@ def paged_attention(q, cache, batch, scale: float | None = None, window: int = 0
     heads_q is a multiple of the cache's heads; query head h reads key head h // (heads_q / heads).
     The row at position p sees keys j <= p, under a ``window`` > 0 only those with p - j < window
     or j < ``sinks``; the new tokens' own keys are expected in the cache (``kv_append``).  ``out``
-    (bf16 of q's shape, own strides), ``lse`` (fp32 [tokens, heads_q]) and ``workspace`` (uint8,
+    (bf16 of q's shape, own strides, no memory of q's), ``lse`` (fp32 [tokens, heads_q]) and ``workspace`` (uint8,
     paged_attention_workspace() elements; one for each call that may run at the same time) are
     allocated when not given, on the stream the call runs on.  Rows that see no key get 0 and
     -inf; padding rows are left as they are.  ``status`` (int32 CUDA tensor) receives FA_ERR_PAGE

@@ -384,7 +384,7 @@ typedef struct {
  * fa_kv_append - writes the new tokens' keys and values into the cache.
  *
  *   k, v     device, bf16 [tokens, heads, d], 16-byte aligned, unit stride along d; token and
- *            head strides in elements, multiples of 8 (the same for k and v).
+ *            head strides in elements, positive multiples of 8 (the same for k and v; ignored for a dimension of 1).
  * With FA_KV_E4M3 a row x is stored as e4m3(x / 2^b), nearest even, where 2^b
  * is the smallest power of two with max |x| <= 448 * 2^b, and e = b + 127 kept
  * within 64 .. 253.  Dividing by it is exact, so only the 4-bit significand
@@ -424,7 +424,7 @@ int fa_kv_read(const fa_kv_cache* cache, const fa_kv_batch* batch, void* k, void
  * own keys are expected in the cache already (fa_kv_append).  Pages that hold no visible key are not read.
  *
  *   q, o     device, bf16 [tokens, heads_q, d], 16-byte aligned, unit stride along d; token
- *            and head strides in elements, multiples of 8.  o must not overlap q (not checked).
+ *            and head strides in elements, positive multiples of 8.  o must not overlap q (not checked).
  *   lse      device, fp32 [tokens, heads_q] dense.
  *   heads_q  a positive multiple of the cache's heads; tokens * heads_q / heads <= 2^31 - 1024.
  *   window, sinks  0 .. 2^30; sinks without a window (window = 0) has no effect.
