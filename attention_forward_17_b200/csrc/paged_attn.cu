@@ -92,8 +92,9 @@ int device_ready(int& sms) {
 constexpr int64_t kWholeKeys = 256;
 
 // The row kernel alone takes sequences of up to this many query rows per key head.  Row kernel
-// and tile kernel in us, 8 key heads: 16 sequences over 4,096, 32 rows: d = 64 bf16 37, 63, d = 128 bf16 57, 73, e4m3 67, 79;
-// 4 over 2,000, 48 rows: 17, 23 and 24, 27 and 28, 27; 16 over 4,096, 64 rows: 63, 63 and 90, 74 and 120, 79.
+// and tile kernel in us, 8 key heads, d = 64 bf16 and e4m3, d = 128 bf16 and e4m3: 16 sequences over 4,096, 32 rows:
+// 38, 62; 42, 63; 57, 72; 65, 81.  4 over 2,000, 48 rows: 17, 22; 18, 23; 24, 28; 27, 28.  16 over 4,096, 64 rows:
+// 65, 61; 73, 63; 90, 73; 115, 81.
 constexpr int64_t kRowLimit = 48;
 
 struct Plan {
@@ -107,6 +108,9 @@ int row_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32
 // kernel takes the smallest tile that holds the longest sequence's rows.  When
 // some sequence may have more than kRowLimit rows, single tokens go to the row
 // kernel and all others to the tile kernel, or all when there is only one sequence.
+// (So a sequence of a few tokens takes the tile kernel when another one of the batch has a chunk, and the row
+// kernel otherwise.  A 700-token chunk among 16 sequences over 4,096, d = 128, bf16 and e4m3: 108 and 98 us with
+// one token each, 117 and 130 with four.  A row kernel for them beside the chunk was not tried.)
 Plan make_plan(const fa_kv_batch* b, int64_t group) {
     const int64_t n = b->max_new < b->tokens ? b->max_new : b->tokens;
     const int64_t rows = n * group;
