@@ -162,7 +162,7 @@ __device__ __forceinline__ uint32_t f16_power(int x) {
 // e4m3 tiles whose scales lie far apart: a softmax thread's whole step, with each key's own scales, in
 // short loops out of line (chunks of 4 sequences over 31,477 cached, d = 128, and 2,048 rows over 16,384, d = 64,
 // where no tile comes here: 576 and 378 us without it; 606 and 426 with it inlined; 580 and 393 called from the
-// step's own loop; 584 and 369 so.  1,515 us when every tile of the first comes here).  S becomes
+// step's own loop; 584 and 369 so.  1,542 us when every tile of the first comes here).  S becomes
 // t_j = s_j + b_j in place.  The row sees the keys below a of the tile that are not below b, or are below z.
 template <int D>
 __device__ __noinline__ void step_by_key(const uint32_t* ek, const uint32_t* ev, uint32_t ts, uint32_t to, int a, int b, int z,
