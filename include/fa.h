@@ -440,9 +440,10 @@ int fa_kv_read(const fa_kv_cache* cache, const fa_kv_batch* batch, void* k, void
  * Products and sums: bf16 (16-bit float for an e4m3 cache) products with fp32 accumulation, fp32
  * softmax, weights rounded to 16 bits before the product with V.  With an e4m3 cache an element of Q below
  * 2^-24 of its row's largest and a cached row at the lowest scale (e = 64: all of it below 2^-54) may count
- * as zero; apart from that cached values enter as they are, whatever the sizes of other rows, as long as V stays
- * below 2^48 (the sum of the weights is held relative to weight times scale, and beside larger rows of V a
- * row of zeros loses its weight; bf16 caches: below 2^80).  LSE is good to about 2^-22 (|LSE| + |log2 of V's scales|).
+ * as zero, and each key's part of O (weight times row of V) is held to 2^-25 of the largest part that the query
+ * sees; rows that it does not see have no part in that.  V has to stay below 2^48 there (the sum of the
+ * weights is held relative to weight times scale, and beside larger rows of V a row of zeros loses its
+ * weight; bf16 caches: below 2^80), and LSE is good to about 2^-22 (|LSE| + |log2 of V's scales|).
  * Results do not depend on the
  * order in which the GPU runs the parts.  Checks in the order of fa_kv_append (heads_q, window
  * and sinks with the sizes, scale after alignment, workspace_bytes too small: FA_ERR_SHAPE).
