@@ -33,12 +33,12 @@
 //
 // Measured on one B200 (device time): a 512-token chunk over 16,384 cached, 8 key heads of 4 query
 // heads, d = 128, bf16: 119 to 122 us with the join, 1,110 to 1,140 TFLOP/s, 0.67 to 0.69 of the measured cuBLAS burst
-// (141 us, 960 TFLOP/s, call after call through the API).  A 256 x 128 step takes about 2,850 cycles against 2,048 of tensor work (the softmax's chain, as in
-// the dense kernel, 1,600 TFLOP/s if it were all); the rest is the start (about 7,000 cycles until
-// the first scores), each segment's end (4,000) and the join.  e4m3: 3,200 cycles a step, since
-// widening shares the issue slots with the softmax.  d = 64: 2,048 rows over 16,384, 376 us bf16 and 368 e4m3, 685 and
-// 700 TFLOP/s, 0.42: the 32,768 exponentials of a step, all on the special-function unit (16 a cycle), take 2,048
-// cycles against 1,024 of tensor work.
+// (141 us, 960 TFLOP/s, call after call through the API).  A 256 x 128 step takes about 2,850 cycles
+// against 2,048 of tensor work (the softmax's chain, as in the dense kernel, 1,600 TFLOP/s if it were all);
+// the rest is the start (about 7,000 cycles until the first scores), each segment's end (4,000) and the join.
+// e4m3: 3,200 cycles a step, since widening shares the issue slots with the softmax.  d = 64: 2,048 rows
+// over 16,384, 376 us bf16 and 368 e4m3, 685 and 700 TFLOP/s, 0.42: the 32,768 exponentials of a step, all on the
+// special-function unit (16 a cycle), take 2,048 cycles against 1,024 of tensor work.
 //
 // Threads: warps 0-3 and 4-7 softmax of the two tiles, 8 producer, 9 issuer, 10
 // tensor memory and scheduling, 11 idle, 12-15 widening (e4m3 only).
@@ -76,7 +76,7 @@ struct Cfg {
     static constexpr int kRawOff = kSlotOff + kSlots * kTileBytes;
     static constexpr int kExpOff = kRawOff + kRaws * kRawBytes;
     static constexpr int kBarOff = kExpOff + kRaws * kExpBytes;
-    static constexpr int kSmemBytes = 1024 + kBarOff + (FP8 ? 3072 : 640);
+    static constexpr int kSmemBytes = 1024 + kBarOff + (FP8 ? 2944 : 640);
     static_assert(kSmemBytes <= 232448 - 512, "shared memory per CTA");
     static constexpr uint32_t kColO = 256;
 };
